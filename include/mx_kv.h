@@ -144,10 +144,9 @@ mx_status mxkv_read(const mxkv_cache* cache, const int32_t* slots, int64_t token
  *  out   : bf16, contiguous batch x new_tokens x q_heads x dim; lse: optional fp32, batch x
  *          new_tokens x q_heads.
  *  workspace: mxkv_attention_workspace_size(...) bytes (contents unspecified before and after).
- * Scores and sums are fp32; the p_j, taken relative to a maximum that may trail the true one by a factor of
- * 2^8, are rounded to bf16 for their product with the values (exact in bf16), which costs each term at most
- * 2^-8 of itself.  The order of
- * sums is fixed by the sizes and lengths: repeated calls give the same bits.
+ * Scores, the p_j and sums are fp32 (the product with the values keeps each p_j to 2^-16 of itself), and the
+ * result is rounded once, to bf16.  The order of sums is fixed by the sizes and lengths: repeated calls give the
+ * same bits.
  * Errors: MX_ERR_INVALID_ARG for null pointers, negative sizes or strides, q_heads not a
  * multiple of heads, a softmax_scale that is not finite, a missing or short workspace;
  * MX_ERR_UNSUPPORTED for batch * new_tokens * q_heads >= 2^24, batch > 65535, or a block table so

@@ -21,8 +21,11 @@
 //
 // The running maximum is raised only when a score passes it by 8 (in powers of two): p then stays
 // below 2^8, sums stay far from overflow, and the accumulators are rarely rescaled.  Sums, maxima and scores
-// are fp32.  Two roundings to bf16 are made: of p, since the product takes bf16 (2^-8 of a term, next to the 4
-// to 7 bits that the values have), and of the result; codes times scales are exact in bf16.
+// are fp32.  The product with the values takes bf16, in which codes times scales are exact and p is not: p goes
+// in as two parts, its nearest bf16 and the nearest bf16 of the rest, which leaves 2^-16 of it.  One part, 2^-8
+// of a term, was as large an error as the rounding of the result, which is the only one to bf16 now.  The second
+// products are free where memory is waited for (32 sequences up to 8192: 41.9 and 42.3 us) and cost the
+// many-row cases 13 to 18% (8 trees over FP8: 68.7 and 77.7 us; 512 rows of a head over 131072 tokens: 389 and 458).
 //
 // What bounds it.  Few rows (decode): HBM, 5.3 TB/s of FP4 and 5.8 of FP8 per added token, and some 6 us of
 // loads that wait for each other before the first tile and after the last.  Many rows: issue.  Over FP4 a tile
@@ -780,9 +783,9 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                 wait_loads<0>();
             }
             // Of two workgroups of a CU the older is served first, and ends early: they take turns in front,
-            // four tiles each (512 rows of a head over 131072 FP8 tokens: 461 to 445 us, 192 rows over 8 x 16384:
-            // 186 to 179).  FP4 lost 1 to 3% by it, and fewer rows, which wait for memory, gained nothing.
-            if constexpr (FP8 && NQ * D == 256) {
+            // four tiles each (512 rows of a head over 131072 FP4 tokens: 488 to 458 us).  Fewer rows, which wait
+            // for memory, gained nothing.
+            if constexpr (NQ * D == 256) {
                 if (((k >> 2) + (blockIdx.x >> 8)) & 1) __builtin_amdgcn_s_setprio(0);
                 else __builtin_amdgcn_s_setprio(1);
             }
@@ -847,7 +850,7 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                     for (int w = 0; w < ST::VW; ++w) v[k][w] = taken ? v[k][w] : 0u;
                 }
             }
-            bf16x8 pr[NQ];
+            bf16x8 pr[NQ], rest[NQ];  // p in two parts, bf16 each
             float top[NQ];
             bool raise = false;
 #pragma unroll
@@ -878,10 +881,15 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                     sum += e[k];
                 }
                 l[i] += sum;
-                u32x4 w;
+                u32x4 w, r;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)e[2 * k], (__bf16)e[2 * k + 1]});
+                for (int k = 0; k < 4; ++k) {
+                    w[k] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)e[2 * k], (__bf16)e[2 * k + 1]});
+                    const float r0 = e[2 * k] - u2f(w[k] << 16), r1 = e[2 * k + 1] - u2f(w[k] & 0xFFFF0000u);
+                    r[k] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)r0, (__bf16)r1});
+                }
                 pr[i] = __builtin_bit_cast(bf16x8, w);
+                rest[i] = __builtin_bit_cast(bf16x8, r);
             }
             for (uint32_t left = uniform(apart); left; left &= left - 1) {
                 const uint32_t t = (uint32_t)__builtin_ctz(left), k = (t >> 4) * 4 + ((t >> 2) & 3);
@@ -889,9 +897,12 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                 float pt[NQ];
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
-                    const u32x4 w = __builtin_bit_cast(u32x4, pr[i]);
-                    const uint32_t both = k & 4 ? (k & 2 ? w[3] : w[2]) : (k & 2 ? w[1] : w[0]);
-                    pt[i] = u2f((uint32_t)__shfl((int)(k & 1 ? both & 0xFFFF0000u : both << 16), (int)from));
+                    auto part = [&](const bf16x8& x) {
+                        const u32x4 w = __builtin_bit_cast(u32x4, x);
+                        const uint32_t both = k & 4 ? (k & 2 ? w[3] : w[2]) : (k & 2 ? w[1] : w[0]);
+                        return u2f(k & 1 ? both & 0xFFFF0000u : both << 16);
+                    };
+                    pt[i] = __shfl(part(pr[i]) + part(rest[i]), (int)from);
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -912,6 +923,11 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                 for (int i = 0; i < NQ; ++i) {
                     o[i][2 * J] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, pr[i], o[i][2 * J], 0, 0, 0);
                     o[i][2 * J + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, pr[i], o[i][2 * J + 1], 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    o[i][2 * J] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, rest[i], o[i][2 * J], 0, 0, 0);
+                    o[i][2 * J + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, rest[i], o[i][2 * J + 1], 0, 0, 0);
                 }
             };
             pv(std::integral_constant<int, 0>{});
