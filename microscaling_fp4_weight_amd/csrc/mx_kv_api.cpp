@@ -3,6 +3,7 @@
 // synchronization, no global state.
 #include "mx_kv.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -11,7 +12,10 @@
 namespace {
 
 constexpr int64_t kMaxDim = 512;
-constexpr int64_t kMaxElems = int64_t(1) << 32;  // of one dense tensor: every unit index stays below 2^31
+// Kernels number their units of work in 31 bits.  Writes and reads have two tensors' elements in units of 8 or
+// 16: below 2^31 for any dense tensor that is accepted.  A rotation may have a unit for each element.
+constexpr int64_t kMaxElems = int64_t(1) << 32;               // of a dense tensor
+constexpr int64_t kMaxRopeElems = (int64_t(1) << 31) - 1;     // of a rotation's launch: larger ones go in parts
 constexpr int64_t kMaxRows = int64_t(1) << 24;   // rows of an attention call
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -135,18 +139,26 @@ mx_status mxkv_rope(const void* x, mx_dtype type, int64_t tokens, int64_t heads,
     if ((st = check_rope(positions, table, max_pos, rot_dim, dim)) != MX_OK) return st;
     if (!aligned16(x) || !aligned16(y)) return MX_ERR_ALIGNMENT;
     mxk::RopeArgs a{};
-    a.x = x;
-    a.y = y;
     a.bf16 = type == MX_BF16;
-    a.tokens = (uint32_t)tokens;
-    a.heads = (uint32_t)heads;
     a.dim = (uint32_t)dim;
     a.ldx_t = ld_x_token;
     a.ldx_h = ld_x_head;
     a.ldy_t = ld_y_token;
     a.ldy_h = ld_y_head;
     a.r = rope_of(positions, table, max_pos, rot_dim, interleaved, transpose);
-    return mxk::launch_rope(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MX_OK : MX_ERR_HIP;
+    const int64_t size = a.bf16 ? 2 : 4;
+    const int64_t some_heads = std::min(heads, kMaxRopeElems / dim), some_tokens = std::min(tokens, kMaxRopeElems / (some_heads * dim));
+    for (int64_t t = 0; t < tokens; t += some_tokens) {
+        for (int64_t h = 0; h < heads; h += some_heads) {
+            a.x = static_cast<const uint8_t*>(x) + (t * ld_x_token + h * ld_x_head) * size;
+            a.y = static_cast<uint8_t*>(y) + (t * ld_y_token + h * ld_y_head) * size;
+            a.tokens = (uint32_t)std::min(some_tokens, tokens - t);
+            a.heads = (uint32_t)std::min(some_heads, heads - h);
+            a.r.positions = rot_dim ? positions + t : nullptr;
+            if (mxk::launch_rope(a, static_cast<hipStream_t>(stream)) != hipSuccess) return MX_ERR_HIP;
+        }
+    }
+    return MX_OK;
 }
 
 mx_status mxkv_write(const mxkv_cache* cache, const void* k, const void* v, mx_dtype type, int64_t tokens,
