@@ -8,7 +8,8 @@
     out = mx.mxkv_attention(q.view(batch, new, q_heads, dim), cache, block_table, lens)
 
 As elsewhere in this package every function only checks and marshals tensors; the arithmetic runs
-in the library's HIP kernels, on the current stream unless one is given.
+in the library's HIP kernels, on the current stream unless one is given.  With a stream given, results that are
+not passed in and the workspace are memory of that stream, and the caller orders it with others.
 """
 from __future__ import annotations
 
@@ -17,6 +18,8 @@ import struct
 from typing import NamedTuple
 
 import torch
+
+from .streams import made_on
 
 ELEMENT = {"fp4": 0, "fp8": 1}
 SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
@@ -82,7 +85,9 @@ def _stream(stream, device: int) -> int:
     device has to be current."""
     if torch._C._cuda_getDevice() != device:
         raise ValueError(f"the tensors are on GPU {device}, the current device is {torch._C._cuda_getDevice()}")
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
 
 
 def _on_gpu(t: torch.Tensor) -> int:
@@ -183,7 +188,7 @@ def mxkv_rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: 
     """cos | sin of position * frequency, (max_pos, rot_dim) fp32.  `scaling` stretches the
     frequencies for long contexts: "linear" divides them by factor, "base" enlarges the base,
     "parts" divides only those that make few turns (between low and high) in original_len positions."""
-    table = torch.empty((max_pos, rot_dim), dtype=_F32, device=device)
+    table = made_on(stream, torch.empty, (max_pos, rot_dim), dtype=_F32, device=device)
     _check(_entry().mxkv_rope_table(table.data_ptr(), max_pos, rot_dim, base, SCALING[scaling], factor, original_len, low,
                                     high, magnitude, _stream(stream, _on_gpu(table))), "mxkv_rope_table")
     return table
@@ -197,17 +202,18 @@ def mxkv_rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, int
     shape, ld = _dense(x, "x")
     tokens, heads, dim = shape
     pos, tab, max_pos, rot = _rope_args(positions, table, tokens, dim)
-    if y is None:
-        y = torch.empty_like(x)  # as dense as x: unit stride along dim
-        ldy = y.stride()
-    else:
+    if y is not None:
         yshape, ldy = _dense(y, "y")
         if yshape != shape or y.dtype is not x.dtype:
             raise ValueError("y must have the shape and dtype of x")
     device = _on_gpu(x)
     _same_device(device, positions, table, y)
+    where = _stream(stream, device)
+    if y is None:
+        y = made_on(stream, torch.empty_like, x)  # as dense as x: unit stride along dim
+        ldy = y.stride()
     st = _entry().mxkv_rope(x.data_ptr(), _TYPE[x.dtype], tokens, heads, dim, ld[0], ld[1], pos, tab, max_pos, rot, interleaved,
-                            transpose, y.data_ptr(), ldy[0], ldy[1], _stream(stream, device))
+                            transpose, y.data_ptr(), ldy[0], ldy[1], where)
     if st:
         _check(st, "mxkv_rope")
     return y
@@ -254,14 +260,17 @@ def mxkv_read(cache, slots: torch.Tensor, block: int = 32, fmt: str = "e8m0", el
     if out_dtype not in _TYPE:
         raise TypeError(f"unsupported dtype {out_dtype}")
     shape = (tokens, heads, dim)
-    if k is None:
-        k = torch.empty(shape, dtype=out_dtype, device=slots.device)
-    if v is None:
-        v = torch.empty_like(k)
-    kp, vp = _like(k, "k", shape, out_dtype), _like(v, "v", shape, out_dtype)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _like(t, name, shape, out_dtype)
     device = _on_gpu(slots)
     _same_device(device, *cache, k, v)
-    st = _entry().mxkv_read(pool, where, tokens, kp, vp, _TYPE[out_dtype], _stream(stream, device))
+    on = _stream(stream, device)
+    if k is None:
+        k = made_on(stream, torch.empty, shape, dtype=out_dtype, device=slots.device)
+    if v is None:
+        v = made_on(stream, torch.empty, shape, dtype=out_dtype, device=slots.device)
+    st = _entry().mxkv_read(pool, where, tokens, k.data_ptr(), v.data_ptr(), _TYPE[out_dtype], on)
     if st:
         _check(st, "mxkv_read")
     return k, v
@@ -308,29 +317,28 @@ def mxkv_attention(q: torch.Tensor, cache, block_table: torch.Tensor, lens: torc
         if mshape != (batch, new, new) and mshape != (1, new, new) or (ldm[2] != 1 and new > 1):
             raise ValueError(f"mask must be a 3-D tensor ({batch} or 1, {new}, {new}) with unit stride along the last")
         mp, mb, mr = mask.data_ptr(), 0 if mshape[0] == 1 else ldm[0], ldm[1]
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        op = out.data_ptr()
-    else:
-        op = _like(out, "out", shape, _BF16)
-    if return_lse and lse is None:
-        lse = torch.empty((batch, new, q_heads), dtype=_F32, device=q.device)
-    ep = None if lse is None else _like(lse, "lse", (batch, new, q_heads), _F32)
+    if out is not None:
+        _like(out, "out", shape, _BF16)
+    if lse is not None:
+        _like(lse, "lse", (batch, new, q_heads), _F32)
     L = _entry()
     need = L.mxkv_attention_workspace_size(pool, batch, new, q_heads, max_pages)
-    wp, wn = None, 0
-    if workspace is not None:
-        if workspace.dtype is not _U8 or not workspace.is_contiguous() or workspace.numel() < need:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes")
-    elif need:
-        workspace = lens.new_empty(need, dtype=_U8)
-    if workspace is not None:
-        wp, wn = workspace.data_ptr(), workspace.numel()
+    if workspace is not None and (workspace.dtype is not _U8 or not workspace.is_contiguous() or workspace.numel() < need):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes")
     device = _on_gpu(q)
     _same_device(device, *cache, block_table, lens, n_new, mask, out, lse, workspace)
+    where = _stream(stream, device)
+    if out is None:
+        out = made_on(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
+    if return_lse and lse is None:
+        lse = made_on(stream, torch.empty, (batch, new, q_heads), dtype=_F32, device=q.device)
+    if workspace is None and need:
+        workspace = made_on(stream, lens.new_empty, need, dtype=_U8)
+    op, ep = out.data_ptr(), None if lse is None else lse.data_ptr()
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     st = L.mxkv_attention(pool, q.data_ptr(), batch, new, q_heads, ldq[0], ldq[1], ldq[2], block_table.data_ptr(), max_pages,
                           ldt[0], lp, np, mp, mb, mr, dim ** -0.5 if softmax_scale is None else softmax_scale, op, ep, wp, wn,
-                          _stream(stream, device))
+                          where)
     if st:
         _check(st, "mxkv_attention")
     return (out, lse) if return_lse else out
