@@ -87,6 +87,8 @@ def _stream(stream, device: int) -> int:
         raise ValueError(f"the tensors are on GPU {device}, the current device is {torch._C._cuda_getDevice()}")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the tensors are on GPU {device}, the stream on GPU {stream.device_index}")
     return stream.cuda_stream
 
 

@@ -87,6 +87,14 @@ def test_cache_calls_make_their_tensors_on_the_given_stream(made, name):
     assert made.on == [None] * count and made.calls[-1][1][-1] == 11
 
 
+def test_cache_calls_refuse_a_stream_of_another_gpu(made):
+    for name, (_, call) in kv_calls().items():
+        before = len(made.calls)
+        with pytest.raises(ValueError, match="stream on GPU 1"):
+            call(stream=SimpleNamespace(cuda_stream=77, device_index=1))
+        assert all(c[0].endswith("workspace_size") for c in made.calls[before:]), name
+
+
 @pytest.mark.gpu
 def test_attention_on_two_streams_without_a_workspace():
     """Both calls wait behind a long kernel when they return; what the current stream allocates and fills then
