@@ -99,7 +99,8 @@ mx_status mxkv_rope(const void* x, mx_dtype type, int64_t tokens, int64_t heads,
  * mxkv_write -- quantize the keys and values of `tokens` tokens into their slots.  With a
  * table (not NULL) the keys are rotated first, exactly as mxkv_rope rotates them (rounding to
  * `type` included).
- *  k, v  : tokens x heads x dim, strides in elements as for mxkv_rope.
+ *  k, v  : tokens x heads x dim, strides in elements as for mxkv_rope; finite, as for mx_quantize (what a slot
+ *          holds that was written from other numbers is unspecified).
  *  slots : tokens int32; a slot outside the pool is passed over (nothing is written for that
  *          token, its k_hat / v_hat rows are written all the same).  Two tokens with the same slot in one
  *          call leave either of the two there.
@@ -134,7 +135,7 @@ mx_status mxkv_read(const mxkv_cache* cache, const int32_t* slots, int64_t token
  * and lse = log sum_j exp(softmax_scale q . k_j).  A token that sees nothing, and a token
  * i >= n_new[b], gives out = 0 and lse = -inf.  Slots past a sequence's tokens are not used,
  * whatever they hold, and a token that does not see new token j is free of what slot j holds, NaN bytes
- * among it.  In a token that is seen, a NaN byte (never written by mxkv_write) of a code or an E8M0 scale
+ * and values past bf16's range among it.  In a token that is seen, a NaN byte (never written by mxkv_write) of a code or an E8M0 scale
  * gives NaN; one of an E4M3 or UE5M3 scale gives NaN or the value of the bits.
  *  q     : batch x new_tokens x q_heads x dim bf16, unit stride along dim, other strides given.
  *  block_table: batch rows of max_pages int32, row stride ld_table.

@@ -484,16 +484,18 @@ __device__ __forceinline__ void value_pair(const uint32_t (&v)[8][VW], const flo
     a1 = __builtin_bit_cast(bf16x8, u32x4{d1[0], d1[1], d1[2], d1[3]});
 }
 
-// Whether a run of codes or its scale has a NaN
+// Whether a run of codes may stand for a value that is not finite in bf16: a NaN byte, or a power of two as its
+// scale under which the format's largest magnitude, 6 or 448, reaches 2^128 -- bytes 253 (2^126) or 247 (2^120) and
+// up, 255 (NaN) among them.  Under E4M3 and UE5M3 scales no value passes 2^26.
 template <bool FP8, bool POW2, int VW>
-__device__ __forceinline__ bool has_nan(const uint32_t (&w)[VW], float s)
+__device__ __forceinline__ bool may_be_infinite(const uint32_t (&w)[VW], float s)
 {
-    bool nan = POW2 && (f2u(s) << 1) >= 0xFF000000u;  // the exponent of byte 0xFF
+    bool yes = POW2 && f2u(s) >= (FP8 ? 247u : 253u) << 23;
     if constexpr (FP8) {
 #pragma unroll
-        for (int i = 0; i < VW; ++i) nan |= (((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+        for (int i = 0; i < VW; ++i) yes |= (((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
     }
-    return nan;
+    return yes;
 }
 
 // The lowest n bits
@@ -831,14 +833,14 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                         hides |= tok[i] < s.fresh && (((here & ~seen) >> bit) & 1u);
                     }
                 }
-                // What lies past the sequence may be anything, NaN among it; so may what some rows do not
+                // What lies past the sequence may be anything, infinite or NaN too; so may what some rows do not
                 // see, and 0 times that would be NaN in them.
                 if (__ballot(hides)) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint64_t nan = __ballot(has_nan<FP8, POW2>(v[k], vs[k]));
+                        const uint64_t lanes = __ballot(may_be_infinite<FP8, POW2>(v[k], vs[k]));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) apart |= (nan >> (16 * i)) & 0xFFFFu ? 1u << (16 * (k >> 2) + 4 * (k & 3) + i) : 0u;
+                        for (int i = 0; i < 4; ++i) apart |= (lanes >> (16 * i)) & 0xFFFFu ? 1u << (16 * (k >> 2) + 4 * (k & 3) + i) : 0u;
                     }
                     apart &= here;
                 }
