@@ -453,14 +453,14 @@ __device__ __forceinline__ uint32_t pair_bf16(const uint32_t* w, float s)
     else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[J / 4], s, J % 4));
 }
 
-// Elements 2 J and on of a value run with scale s, times p, to sums r of o; p is 0 in rows that do not see it
+// Elements 2 J and on of a value run with scale s, times p, to sums r of o, in rows that see the token
 template <bool FP8, int J = 0, int VW, int NJ>
-__device__ __forceinline__ void add_run(const uint32_t (&w)[VW], float s, float p, f32x4 (&o)[NJ], int r)
+__device__ __forceinline__ void add_run(const uint32_t (&w)[VW], float s, float p, bool sees, f32x4 (&o)[NJ], int r)
 {
     const f32x2 e = pair_f32<FP8, J>(w);
-    o[2 * J][r] += p != 0.f ? e.x * s * p : 0.f;
-    o[2 * J + 1][r] += p != 0.f ? e.y * s * p : 0.f;
-    if constexpr (2 * J + 2 < NJ) add_run<FP8, J + 1>(w, s, p, o, r);
+    o[2 * J][r] += sees ? e.x * s * p : 0.f;
+    o[2 * J + 1][r] += sees ? e.y * s * p : 0.f;
+    if constexpr (2 * J + 2 < NJ) add_run<FP8, J + 1>(w, s, p, sees, o, r);
 }
 
 // value operands of elements 2 J and 2 J + 1: 8 tokens each
@@ -820,17 +820,18 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                     for (int i = 0; i < NQ; ++i) x[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, q[i][st], x[i][h], 0, 0, 0);
                 }
             uint32_t apart = 0;  // tokens whose values are added to the rows that see them, and to no others
+            uint32_t seen[NQ];  // bits of the tokens that a row sees, of the new ones those of the lane's group
             if (__builtin_expect(edge, 0)) {
                 const uint32_t g = fresh(lane >> 4);
                 bool hides = false;
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
-                    const uint32_t seen = seen_bits(a, s, b, tok[i], t0, here, g, pack ? masks[tok[i] < s.fresh ? tok[i] - tok0 : 0u] : nullptr);
+                    seen[i] = seen_bits(a, s, b, tok[i], t0, here, g, pack ? masks[tok[i] < s.fresh ? tok[i] - tok0 : 0u] : nullptr);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint32_t bit = 16 * (k >> 2) + 4 * (k & 3) + g;
-                        if (!((seen >> bit) & 1u)) x[i][k >> 2][k & 3] = -INFINITY;
-                        hides |= tok[i] < s.fresh && (((here & ~seen) >> bit) & 1u);
+                        if (!((seen[i] >> bit) & 1u)) x[i][k >> 2][k & 3] = -INFINITY;
+                        hides |= tok[i] < s.fresh && (((here & ~seen[i]) >> bit) & 1u);
                     }
                 }
                 // What lies past the sequence may be anything, infinite or NaN too; so may what some rows do not
@@ -897,8 +898,10 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                 const uint32_t t = (uint32_t)__builtin_ctz(left), k = (t >> 4) * 4 + ((t >> 2) & 3);
                 const uint32_t lane = fresh(threadIdx.x & 63), from = 16 * (t & 3) + (lane & 15);  // the lane with this row's p of t
                 float pt[NQ];
+                bool sees[NQ];  // not p != 0: of a token that is seen, NaN counts at any weight
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
+                    sees[i] = ((uint32_t)__shfl((int)seen[i], (int)from) >> t) & 1u;
                     auto part = [&](const bf16x8& x) {
                         const u32x4 w = __builtin_bit_cast(u32x4, x);
                         const uint32_t both = k & 4 ? (k & 2 ? w[3] : w[2]) : (k & 2 ? w[1] : w[0]);
@@ -913,7 +916,7 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                     ST::value_run(at, t >> 4, t & 15, m, run);
                     const float f = nan_scale<POW2>(scale_f32<POW2>(p, ST::scale(p, at, 1, t, m * NJ)));
 #pragma unroll
-                    for (int i = 0; i < NQ; ++i) add_run<FP8>(run, f, pt[i], o[i], r);
+                    for (int i = 0; i < NQ; ++i) add_run<FP8>(run, f, pt[i], sees[i], o[i], r);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);  // the values are not decoded before their turn

@@ -90,3 +90,26 @@ def test_tokens_written_from_values_that_are_not_finite(element, dim, bad):
         got = mx.mxkv_attention(q, poked, mask=mask, **kind)
         hidden = torch.from_numpy(~sees[:, BAD]).to(DEV)
         assert torch.equal(got[0, hidden], want[0, hidden])
+
+
+@pytest.mark.parametrize("q_heads", [2, 6, 12])
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("element", ["fp4", "fp8"])
+def test_a_seen_nan_is_nan_whatever_its_weight(element, dim, q_heads):
+    """A NaN value under a score far below the row's maximum, so that its weight is 0: the rows that see it are NaN, as
+    they are where nobody hides it, and the others keep their bits."""
+    new = 20
+    rng, cache, q, kind, (page, place) = case(dim, q_heads, element=element)
+    q[:] = 40.0 * torch.sign(q[:, :1, :1])
+    poked = mx.KVCache(*(t.clone() for t in cache))
+    low = torch.where(q[0, 0, 0] > 0, -6.0, 6.0).bfloat16().expand(1, 2, dim).contiguous()  # scores of -240 dim^0.5
+    mx.mxkv_write(low, low, poked, ints([page * PAGE + place]), block=16, element=element)
+    free = mx.KVCache(*(t.clone() for t in poked))
+    poked[3][page, :, place] = 0xFF
+    nobody = np.ones((new, new), dtype=bool)
+    for mask, sees in [*masks(rng, new), (torch.from_numpy(nobody[None]).to(DEV), nobody)]:
+        want = mx.mxkv_attention(q, free, mask=mask, **kind)
+        got = mx.mxkv_attention(q, poked, mask=mask, **kind)
+        hidden = torch.from_numpy(~sees[:, BAD]).to(DEV)
+        assert torch.isfinite(want.float()).all() and torch.equal(got[0, hidden], want[0, hidden])
+        assert torch.isnan(got[0, ~hidden]).all()
