@@ -102,8 +102,8 @@ mx_status mxkv_rope(const void* x, mx_dtype type, int64_t tokens, int64_t heads,
  *  k, v  : tokens x heads x dim, strides in elements as for mxkv_rope; finite, as for mx_quantize (what a slot
  *          holds that was written from other numbers is unspecified).
  *  slots : tokens int32; a slot outside the pool is passed over (nothing is written for that
- *          token, its k_hat / v_hat rows are written all the same).  Two tokens with the same slot in one
- *          call leave either of the two there.
+ *          token, its k_hat / v_hat rows are written all the same).  What a slot holds that two tokens of one
+ *          call share is unspecified: codes and scale bytes of both, mixed.
  *  k_hat, v_hat: optional outputs (both or neither), contiguous tokens x heads x dim of `type`: the values
  *          that the written codes stand for, rounded as mx_dequantize rounds them.
  * Errors: MX_ERR_INVALID_ARG, MX_ERR_UNSUPPORTED and MX_ERR_ALIGNMENT as above; a cache whose

@@ -226,8 +226,9 @@ def mxkv_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, blo
                table: torch.Tensor | None = None, interleaved: bool = False, k_hat: torch.Tensor | None = None,
                v_hat: torch.Tensor | None = None, stream=None):
     """Quantize the keys and values (tokens, heads, dim; bf16 or fp32) of `tokens` tokens into their
-    slots (int32; a negative slot is passed over).  With a table the keys are rotated first, as
-    mxkv_rope does.  k_hat and v_hat, if given (both), receive the values that the codes stand for."""
+    slots (int32; one outside the pool is passed over, and no two tokens of a call may share one).  With a
+    table the keys are rotated first, as mxkv_rope does.  k_hat and v_hat, if given (both), receive the
+    values that the codes stand for."""
     heads, dim, pool = _pool(cache, block, fmt, element, k_scale, v_scale)
     shape, ldk = _dense(k, "k")
     vshape, ldv = _dense(v, "v")
