@@ -69,7 +69,8 @@ __global__ __launch_bounds__(256) void attn_row_kernel(KvAttnArgs a, FastDiv pag
             x += q[k].x * v.x + q[k].y * v.y;
         }
         for (int off = 32; off; off >>= 1) x += __shfl_xor(x, off);
-        const float top = fmaxf(m, x), f = exp2f(m - top), p = exp2f(x - top);
+        // while no score is above -inf all weights are 0
+        const float top = fmaxf(m, x), base = top == -INFINITY ? 0.f : top, f = exp2f(m - base), p = exp2f(x - base);
         m = top;
         l = l * f + p;
 #pragma unroll

@@ -113,3 +113,22 @@ def test_a_seen_nan_is_nan_whatever_its_weight(element, dim, q_heads):
         hidden = torch.from_numpy(~sees[:, BAD]).to(DEV)
         assert torch.isfinite(want.float()).all() and torch.equal(got[0, hidden], want[0, hidden])
         assert torch.isnan(got[0, ~hidden]).all()
+
+
+@pytest.mark.parametrize("element,scale", [("fp4", 0xFE), ("fp8", 0xFE), ("fp8", 0xF9)])
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+def test_keys_that_score_minus_infinity_have_no_weight(element, scale, dim):
+    """Keys past the range of fp32 on the side where scores are -inf, the first of a sequence among them: the
+    same bits as with keys whose scores are finite and have no weight either."""
+    rng, cache, q, kind, _ = case(dim, 6, element=element)
+    q = q.abs() + 0.01
+    first = kind["block_table"][0, 0].item()
+    results = []
+    for byte in (scale, 0x90):
+        poked = mx.KVCache(*(t.clone() for t in cache))
+        for place in (0, 1, 2, 3, 9):
+            poked[0][first, :, place] = 0xFF if element == "fp4" else 0xFE  # -6, -448
+            poked[1][first, :, place] = byte
+        results.append(mx.mxkv_attention(q, poked, return_lse=True, **kind))
+    assert torch.isfinite(results[1][0].float()).all()
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
