@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256) void attn_row_kernel(KvAttnArgs a, FastDiv pag
     const float inv = some ? a.c.g[1] / sum : 0.f;
     for (uint32_t d = threadIdx.x; d < a.c.dim; d += 256) {
         float x = 0.f;
-        for (int w = 0; w < 4; ++w) x += f[w] != 0.f ? part[w][d] * f[w] : 0.f;
+        for (int w = 0; w < 4; ++w) x += part[w][d] * f[w];  // NaN of a wave counts at any weight
         reinterpret_cast<__bf16*>(a.out)[(uint64_t)row * a.c.dim + d] = (__bf16)(some ? x * inv : 0.f);
     }
     if (a.lse && threadIdx.x == 0) a.lse[row] = some ? top * LN2 + logf(sum) : -INFINITY;

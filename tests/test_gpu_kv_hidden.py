@@ -132,3 +132,22 @@ def test_keys_that_score_minus_infinity_have_no_weight(element, scale, dim):
         results.append(mx.mxkv_attention(q, poked, return_lse=True, **kind))
     assert torch.isfinite(results[1][0].float()).all()
     assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+def test_a_seen_nan_is_nan_among_tokens_of_no_weight(dim):
+    """Every fourth or thirty-second token far below the row's maximum, one of them of NaN values."""
+    rng, cache, q, kind, _ = case(dim, 6)
+    q[:] = 40.0 * torch.sign(q[:, :1, :1])
+    low = torch.where(q[0, 0, 0] > 0, -6.0, 6.0).bfloat16()
+    table = kind["block_table"][0]
+    for step in (4, 32):
+        poked = mx.KVCache(*(t.clone() for t in cache))
+        tokens = torch.arange(2, HELD + 20, step, device=DEV)
+        slots = table[tokens // PAGE] * PAGE + (tokens % PAGE).int()
+        rows = low.expand(len(tokens), 2, dim).contiguous()
+        mx.mxkv_write(rows, rows, poked, slots, block=16)
+        assert torch.isfinite(mx.mxkv_attention(q, poked, **kind).float()).all()
+        at = int(slots[1])
+        poked[3][at // PAGE, :, at % PAGE] = 0xFF
+        assert torch.isnan(mx.mxkv_attention(q, poked, **kind)).all()
