@@ -144,8 +144,10 @@ kv::AttnPlan plan_of(const KvAttnArgs& a)
     p.group_div = FastDiv::make(p.group);
     while ((1u << p.block_shift) < a.c.block) ++p.block_shift;
     while ((a.c.block << p.scale_shift) < a.c.dim) ++p.scale_shift;
-    // not 0, so that a score of -inf (a key that is not seen) stays that
-    p.c = fmaxf(fabsf(a.scale) * a.c.g[0] * kv::LOG2E, 1e-30f);
+    // not 0, so that a score of -inf (a key that is not seen) stays that; any other product counts, however small,
+    // since keys may be as large as it is small
+    p.c = fabsf(a.scale) * a.c.g[0] * kv::LOG2E;
+    if (p.c == 0.f) p.c = 0x1p-149f;
     p.flip = a.scale < 0.f ? 0x80008000u : 0u;
     p.s_bits = a.c.fmt == FMT_E4M3 ? 0x7Fu : 0xFFu;
     p.s_sign = a.c.fmt == FMT_E4M3 ? 0x80u : 0u;

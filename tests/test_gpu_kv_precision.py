@@ -7,7 +7,7 @@ import torch
 import kv_util as ku
 import microscaling_fp4_weight_amd as mx
 from gpu_util import DEV
-from test_gpu_kv import KINDS, dev, host, ints, make_cache, sequence
+from test_gpu_kv import KINDS, check_attention, dev, host, ints, make_cache, sequence
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,11 @@ def test_formats(dim, element, fmt, block):
 def test_cut_sequences(new, q_size):
     """Sequences that several workgroups share, with flat and with nearly one-hot weights."""
     check(new, [700, 2500], new, 8, 2, 128, page=64, q_size=q_size)
+
+
+@pytest.mark.parametrize("g", [(1e-32, 1e-32), (1e-32, 3.0), (1e-25, 1e25), (1e30, 1e-30), (1e30, 1e30)])
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+def test_per_tensor_scales_far_from_one(dim, g):
+    """Scores are the same whatever part of a key's size its per-tensor scale carries."""
+    for element in ("fp4", "fp8"):
+        check_attention(np.random.default_rng(dim), [100, 9], 4, 8, 2, dim, element, block=16, g=g)
