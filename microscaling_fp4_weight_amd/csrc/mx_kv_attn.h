@@ -554,17 +554,19 @@ __device__ __forceinline__ float nan_scale(float s)
 
 // Workgroups of a CU (waves of a SIMD) that registers and LDS leave room for, and tiles that a wave's
 // ring in LDS holds: 164 registers for 16 rows of 128 elements, 237 to 246 for 32.
-constexpr int LDS_BYTES = 160 * 1024, LDS_OTHER = 2048;
+constexpr int LDS_BYTES = 160 * 1024;
 constexpr int least(int a, int b) { return a < b ? a : b; }
 template <bool FP8, int D, int BS, int NQ, int SPREAD>
 struct Room {
     using ST = Stage<FP8, D, BS, SPREAD>;
+    static constexpr int OTHER = 1024 * (NQ < 2 ? 2 : NQ);  // what else the kernel has in LDS
     static constexpr int REGISTERS = NQ * D <= 64 ? 4 : (NQ * D <= 128 ? 3 : 2);
-    static constexpr int LDS = LDS_BYTES / (8 * ST::BYTES + LDS_OTHER);  // with two tiles of each wave
+    static constexpr int LDS = LDS_BYTES / (8 * ST::BYTES + OTHER);  // with two tiles of each wave
     static constexpr int GROUPS = LDS < 1 ? 1 : least(LDS, REGISTERS);
-    static constexpr int DEPTH = least(3, (LDS_BYTES / GROUPS - LDS_OTHER) / (4 * ST::BYTES));
+    static constexpr int DEPTH = least(3, (LDS_BYTES / GROUPS - OTHER) / (4 * ST::BYTES));
     static constexpr int RING = 4 * DEPTH * ST::BYTES, JOIN = 4 * NQ * D * 64;
     static constexpr int DYNAMIC = RING > JOIN ? RING : JOIN;
+    static_assert(GROUPS * (DYNAMIC + OTHER) <= LDS_BYTES);
 };
 
 // SPREAD: as for Stage.  The table's entries of a tile's tokens are then read a tile before they are needed and
@@ -578,6 +580,7 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
     extern __shared__ __attribute__((aligned(16))) uint8_t ring[];
     __shared__ float wm[4][ROWS], wl[4][ROWS];
     __shared__ uint32_t masks[ROWS][MASK_BITS / 32];
+    static_assert(sizeof(wm) + sizeof(wl) + sizeof(masks) <= (Room<FP8, D, BS, NQ, SPREAD>::OTHER));
     const uint32_t lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const uint32_t wave = uniform(threadIdx.x >> 6);
 
