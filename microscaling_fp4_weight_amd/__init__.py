@@ -3,7 +3,8 @@
 A thin ctypes binding over libmx.so, whose C ABI is declared in include/mx.h and, for the
 key/value cache (kv.py), include/mx_kv.h.  Every function here only marshals torch tensors (device
 memory) and the current HIP stream into that ABI: all arithmetic runs in the library's HIP
-kernels.  There is no CPU fallback; importing this package without a built libmx.so raises.
+kernels.  A function that is given a stream makes its results and workspace in memory of that stream.
+There is no CPU fallback; importing this package without a built libmx.so raises.
 
     import microscaling_fp4_weight_amd as mx
     codes, scales = mx.mx_quantize(w, block=32, fmt="e8m0")          # w: (n, k) bf16 / f32 on GPU
@@ -19,6 +20,7 @@ import torch
 
 from .kv import (KVCache, mxkv_alloc, mxkv_attention, mxkv_attention_workspace_size, mxkv_read, mxkv_rope,
                  mxkv_rope_table, mxkv_write)
+from .streams import made_on
 
 __all__ = ["mx_quantize", "mx_dequantize", "mx_gemm", "mx_gemm_workspace_size", "mx_scale_bytes",
            "mx_quant_error", "mx_quant_error_workspace_size",
@@ -173,13 +175,13 @@ def mx_quantize(x: torch.Tensor, block: int, fmt: str, tensor_scale: float = 1.0
     rows, k, ld = _rows_ld(x, "x")
     _need_dtype(x, "x", (torch.bfloat16, torch.float32))
     if codes is None:
-        codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
+        codes = made_on(stream, torch.empty, (rows, k // 2), dtype=torch.uint8, device=x.device)
     if scales is None:
         if layout == "rowmajor":
-            scales = torch.empty((rows, k // max(block, 1)), dtype=torch.uint8, device=x.device)
+            scales = made_on(stream, torch.empty, (rows, k // max(block, 1)), dtype=torch.uint8, device=x.device)
         else:
-            scales = torch.empty(max(mx_scale_bytes(rows, k, block, layout), 1), dtype=torch.uint8,
-                                 device=x.device)
+            scales = made_on(stream, torch.empty, max(mx_scale_bytes(rows, k, block, layout), 1),
+                             dtype=torch.uint8, device=x.device)
     _need_bytes(codes, "codes", rows * (k // 2))
     _need_bytes(scales, "scales", mx_scale_bytes(rows, k, block, layout))
     _need_gpu(x=x, codes=codes, scales=scales)
@@ -200,7 +202,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, k: int, block: int,
     _need_bytes(codes, "codes", rows * (k // 2))
     _need_bytes(scales, "scales", mx_scale_bytes(rows, k, block, layout))
     if y is None:
-        y = torch.empty((rows, k), dtype=out_dtype, device=codes.device)
+        y = made_on(stream, torch.empty, (rows, k), dtype=out_dtype, device=codes.device)
     _need_dtype(y, "y", (torch.bfloat16, torch.float32))
     _need_shape(y, "y", (rows, k))
     _, _, ld = _rows_ld(y, "y")
@@ -234,13 +236,13 @@ def mx_quant_error(x: torch.Tensor, block: int, fmt: str, tensor_scale: float = 
             raise ValueError("x_hat must have the shape and dtype of x")
         _, _, ldh = _rows_ld(x_hat, "x_hat")
     if out is None:
-        out = torch.zeros(8, dtype=torch.float64, device=x.device)  # 7 used; 16-byte aligned
+        out = made_on(stream, torch.zeros, 8, dtype=torch.float64, device=x.device)  # 7 used; 16-byte aligned
     _need_dtype(out, "out", (torch.float64,))
     if not out.is_contiguous() or out.numel() < 7:
         raise ValueError("out must be a contiguous float64 tensor of at least 7 elements")
     need = mx_quant_error_workspace_size(rows, k, block)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = made_on(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=x.device)
     _need_bytes(workspace, "workspace", need)
     _need_gpu(x=x, x_hat=x_hat, out=out, workspace=workspace)
     st = lib().mx_quant_error(_ptr(x), _dtype_code(x.dtype), rows, k, ld, block, FMT[fmt], tensor_scale,
@@ -261,13 +263,13 @@ def mx_tensor_stats(x: torch.Tensor, out: torch.Tensor | None = None,
     rows, k, ld = _rows_ld(x, "x")
     _need_dtype(x, "x", (torch.bfloat16, torch.float32))
     if out is None:
-        out = torch.zeros(4, dtype=torch.float64, device=x.device)  # 3 used; 16-byte aligned
+        out = made_on(stream, torch.zeros, 4, dtype=torch.float64, device=x.device)  # 3 used; 16-byte aligned
     _need_dtype(out, "out", (torch.float64,))
     if not out.is_contiguous() or out.numel() < 3:
         raise ValueError("out must be a contiguous float64 tensor of at least 3 elements")
     need = mx_tensor_stats_workspace_size(rows, k)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = made_on(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=x.device)
     _need_bytes(workspace, "workspace", need)
     _need_gpu(x=x, out=out, workspace=workspace)
     st = lib().mx_tensor_stats(_ptr(x), _dtype_code(x.dtype), rows, k, ld, _ptr(out), _ptr(workspace),
@@ -294,9 +296,9 @@ def mx_quantize_fp8(x: torch.Tensor, block: int, fmt: str, tensor_scale: float =
     rows, k, ld = _rows_ld(x, "x")
     _need_dtype(x, "x", (torch.bfloat16, torch.float32))
     if codes is None:
-        codes = torch.empty((rows, k), dtype=torch.uint8, device=x.device)
+        codes = made_on(stream, torch.empty, (rows, k), dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty((rows, k // block if block else 0), dtype=torch.uint8, device=x.device)
+        scales = made_on(stream, torch.empty, (rows, k // block if block else 0), dtype=torch.uint8, device=x.device)
     _need_bytes(codes, "codes", rows * k)
     _need_bytes(scales, "scales", mx_scale_bytes(rows, k, block))
     _need_gpu(x=x, codes=codes, scales=scales)
@@ -315,7 +317,7 @@ def mx_dequantize_fp8(codes: torch.Tensor, scales: torch.Tensor, block: int, fmt
     _need_bytes(codes, "codes", rows * k)
     _need_bytes(scales, "scales", mx_scale_bytes(rows, k, block))
     if y is None:
-        y = torch.empty((rows, k), dtype=out_dtype, device=codes.device)
+        y = made_on(stream, torch.empty, (rows, k), dtype=out_dtype, device=codes.device)
     _need_dtype(y, "y", (torch.bfloat16, torch.float32))
     _need_shape(y, "y", (rows, k))
     _, _, ldy = _rows_ld(y, "y")
@@ -338,7 +340,7 @@ def mx_gemm_fp8(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, 
     _need_bytes(w_codes, "w_codes", n * k)
     _need_bytes(w_scales, "w_scales", mx_scale_bytes(n, k, block))
     if y is None:
-        y = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        y = made_on(stream, torch.empty, (m, n), dtype=out_dtype, device=x.device)
     _need_dtype(y, "y", (torch.bfloat16, torch.float32))
     _need_shape(y, "y", (m, n))
     _, _, ldy = _rows_ld(y, "y")
@@ -370,13 +372,13 @@ def mx_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, bloc
     _need_bytes(w_codes, "w_codes", n * (k // 2))
     _need_bytes(w_scales, "w_scales", mx_scale_bytes(n, k, block, layout))
     if y is None:
-        y = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        y = made_on(stream, torch.empty, (m, n), dtype=out_dtype, device=x.device)
     _need_dtype(y, "y", (torch.bfloat16, torch.float32))
     _need_shape(y, "y", (m, n))
     _, _, ldy = _rows_ld(y, "y")
     need = mx_gemm_workspace_size(m, n, k, block, mode)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = made_on(stream, torch.empty, need, dtype=torch.uint8, device=x.device)
     if workspace is not None:
         _need_bytes(workspace, "workspace", need)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -402,7 +404,7 @@ def mx_gemm_static(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tenso
     _need_bytes(w_codes, "w_codes", n * (k // 2))
     _need_bytes(w_scales, "w_scales", mx_scale_bytes(n, k, block, layout))
     if y is None:
-        y = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        y = made_on(stream, torch.empty, (m, n), dtype=out_dtype, device=x.device)
     _need_dtype(y, "y", (torch.bfloat16, torch.float32))
     _need_shape(y, "y", (m, n))
     _, _, ldy = _rows_ld(y, "y")

@@ -87,6 +87,35 @@ def test_cache_calls_make_their_tensors_on_the_given_stream(made, name):
     assert made.on == [None] * count and made.calls[-1][1][-1] == 11
 
 
+def weight_calls():
+    z = torch.zeros
+    x, codes, bytes8 = z((4, 64), dtype=BF16), z((4, 32), dtype=torch.uint8), z((4, 64), dtype=torch.uint8)
+    scales = z(512, dtype=torch.uint8)
+    return {"quantize": (2, lambda **kw: mx.mx_quantize(x, 32, "e8m0", **kw)),
+            "quantize, tiled": (2, lambda **kw: mx.mx_quantize(x, 32, "e8m0", layout="tiled", **kw)),
+            "dequantize": (1, lambda **kw: mx.mx_dequantize(codes, scales, 64, 32, "e8m0", **kw)),
+            "error": (2, lambda **kw: mx.mx_quant_error(x, 32, "e8m0", **kw)),
+            "statistics": (2, lambda **kw: mx.mx_tensor_stats(x, **kw)),
+            "quantize to FP8": (2, lambda **kw: mx.mx_quantize_fp8(x, 32, "e8m0", **kw)),
+            "dequantize from FP8": (1, lambda **kw: mx.mx_dequantize_fp8(bytes8, scales, 32, "e8m0", **kw)),
+            "product with FP8": (1, lambda **kw: mx.mx_gemm_fp8(x, bytes8, scales, 32, "e8m0", **kw)),
+            "product": (2, lambda **kw: mx.mx_gemm(x, codes, scales, 32, "e8m0", mode="a4", **kw)),
+            "product, static scratch": (1, lambda **kw: mx.mx_gemm_static(x, codes, scales, 32, "e8m0", mode="a4", **kw))}
+
+
+@pytest.mark.parametrize("name", list(weight_calls()))
+def test_weight_calls_make_their_tensors_on_the_given_stream(made, name, monkeypatch):
+    count, call = weight_calls()[name]
+    monkeypatch.setattr(mx, "_need_bytes", lambda *a: None)  # the stand-in's sizes are no sizes
+    side = SimpleNamespace(cuda_stream=77, device_index=0)
+    made.on.clear()
+    call(stream=side)
+    assert made.on == [side] * count and made.calls[-1][1][-1] == 77
+    made.on.clear()
+    call()
+    assert made.on == [None] * count and made.calls[-1][1][-1] == 11
+
+
 def test_cache_calls_refuse_a_stream_of_another_gpu(made):
     for name, (_, call) in kv_calls().items():
         before = len(made.calls)
@@ -143,3 +172,31 @@ def test_rotate_write_and_read_on_a_stream():
     torch.cuda.current_stream().wait_stream(side)
     for a, b, f in zip(*results, filled):
         assert torch.equal(a, b) and (f == 7.0).all()
+
+
+@pytest.mark.gpu
+def test_weight_calls_on_a_stream():
+    """The error split and the statistics (whose results are zeroed first) and a product with its workspace, behind a
+    long kernel, with the current stream's memory filled meanwhile."""
+    from test_gpu_kv import dev
+    x = dev(np.random.default_rng(4).standard_normal((128, 512)), "bf16")
+    side = torch.cuda.Stream()
+    results = []
+    for stream in (None, side):
+        side.wait_stream(torch.cuda.current_stream())
+        if stream is not None:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+        codes, scales = mx.mx_quantize(x, 32, "e8m0", stream=stream)
+        bytes8, scales8 = mx.mx_quantize_fp8(x, 32, "e8m0", stream=stream)
+        results.append([codes, scales, bytes8, scales8, mx.mx_dequantize(codes, scales, 512, 32, "e8m0", stream=stream),
+                        mx.mx_quant_error(x, 32, "e8m0", stream=stream), mx.mx_tensor_stats(x, stream=stream),
+                        mx.mx_dequantize_fp8(bytes8, scales8, 32, "e8m0", stream=stream),
+                        mx.mx_gemm(x, codes, scales, 32, "e8m0", mode="a4", stream=stream),
+                        mx.mx_gemm_fp8(x, bytes8, scales8, 32, "e8m0", stream=stream)])
+        filled = [torch.full_like(t, 7) for t in results[-1]]
+        filled += [torch.full((mx.mx_gemm_workspace_size(128, 128, 512, 32, "a4"),), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert all((f == 7).all() for f in filled)
