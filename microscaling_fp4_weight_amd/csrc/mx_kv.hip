@@ -10,10 +10,11 @@
 // Read: e * s * g rounded once to fp32, then to the output type.
 //
 // All of these move each byte once and do a few operations on it: HBM bounds the large calls (a copy reaches
-// 5.15 TB/s here), the launch the small ones (2.1 us for a rotation of one token, 3.6 for a read or write).
-// Rotations run at 5.6 to 5.9 TB/s, reads at 5.6; writes at 4.7 (8192 x 8 heads of 128 to FP4) and 3.7 (FP8
-// under 16-element E4M3 scales): 64- or 32-byte rows of codes and 4-byte rows of scales, scattered over the
-// pool by slot, are what is left of their time.
+// 5.2 TB/s here), the launch the small ones (2.1 us for a rotation of one token, 3.4 to 3.7 for a read or write).
+// Times here are of calls back to back on three sets of inputs.  Rotations of whole chunks run at 5.8 to 6.0
+// TB/s, reads at 5.7 to 6.0; writes at 4.7 (8192 x 8 heads of 128 to FP4) and 3.9 (FP8 under 16-element E4M3
+// scales): 64- or 32-byte rows of codes and 4-byte rows of scales, scattered over the pool by slot, are what is
+// left of their time.
 #include "mx_device.h"
 #include "mx_fp8_device.h"
 #include "mx_kv_internal.h"
@@ -172,7 +173,8 @@ __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a, RopeGrid g)
     if (two) store_chunk<BF16>(y + d1 * ES, q);
 }
 
-// Any sizes and strides: a thread takes one pair, or one element that is copied.
+// Any sizes and strides: a thread takes one pair, or one element that is copied.  What bounds it is the number of
+// its 2- or 4-byte accesses: 24 of 96 elements, 8192 x 64 heads, bf16, take 150 us, 1.3 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(THREADS) void rope_any_kernel(RopeArgs a, RopeGrid g)
 {
@@ -344,10 +346,10 @@ struct KvGrid {
 
 // The token, tensor and head of row `row` of the grid.  Rows run over 2^token_shift tokens of one head, then
 // over heads: neighbouring tokens' codes and scale bytes share lines of the pool, which one
-// workgroup should touch, not eight on eight L2s.  Four tokens: E4M3 codes of 64-element heads under
-// scales of 16 are written in 24.0 us against 27.0 one token at a time (4099 x 32 heads, bf16), read in
-// 17.9 against 19.2; more tokens of a head at once read their rotation table rows from farther away
-// (16: 20.7 against 18.9 us for 8192 x 8 heads of 128).
+// workgroup should touch, not eight on eight L2s.  E4M3 codes of 64-element heads under scales of 16 (4099 x 32
+// heads, bf16): written in 21.9 us by four tokens, 22.7 one at a time, read in 11.5 by 32 against 14.0.  More
+// tokens of a head at once read their rotation table rows from farther away (16: 17.8 against 17.1 us for 8192 x 8
+// heads of 128 to FP4).
 __device__ __forceinline__ void place_of(const KvGrid& g, uint32_t heads, uint32_t row, uint32_t& token, uint32_t& t, uint32_t& head)
 {
     const uint32_t q = row >> g.token_shift, group = g.rows_div.div(q), th = q - group * g.rows;
@@ -430,7 +432,7 @@ __device__ __forceinline__ void chunks_of(uint32_t u, uint32_t dim, uint32_t rot
 
 // A thread takes CHUNKS times 8 consecutive elements of one head's key or value; a block's absmax
 // comes together by lane shuffles (a block is 2 to 32 adjacent threads: chunks come in whole blocks, so that
-// blocks never straddle a wave).  8192 x 8 heads of 128, bf16 to FP4 and the values back: 17.0 us, 4.7 TB/s.
+// blocks never straddle a wave).  8192 x 8 heads of 128, bf16 to FP4 and the values back: 17.1 us, 4.7 TB/s.
 template <bool FP8, int FMT, bool G1, bool BF16, int CHUNKS, bool WAVES>
 __global__ __launch_bounds__(THREADS) void kv_write_kernel(KvWriteArgs a, KvGrid g)
 {
@@ -535,7 +537,7 @@ __global__ __launch_bounds__(THREADS) void kv_write_kernel(KvWriteArgs a, KvGrid
 }
 
 // A thread takes two chunks of 8 elements, half a row apart; of 32 neighbouring tokens the rows of one head lie
-// together.  16384 x 8 heads of 128 from FP4 to bf16: 15.1 us, 5.6 TB/s.
+// together.  16384 x 8 heads of 128 from FP4 to bf16: 15.0 us, 5.7 TB/s.
 template <bool FP8, int FMT, bool G1, bool BF16>
 __global__ __launch_bounds__(THREADS) void kv_read_kernel(KvReadArgs a, KvGrid g)
 {
@@ -576,9 +578,9 @@ KvGrid kv_grid(const KvPool& c, uint32_t tokens, uint32_t chunks, uint32_t token
     g.lanes = c.block / 8;
     while ((1u << g.block_shift) < c.block) ++g.block_shift;
     // A write with a power of two of threads a row, and heads in whole waves: a wave stays with one token, and its
-    // slot, position and addresses are scalar: 17.0 us against 17.9 for 8192 x 8 heads of 128 (bf16 to FP4 and
-    // back), 32.8 against 36.4 in fp32.  A read has too little of that to gain: 15.1 us either way for twice the
-    // tokens, FP8 17.9 against 17.3.
+    // slot, position and addresses are scalar: 17.1 us against 18.1 for 8192 x 8 heads of 128 (bf16 to FP4 and
+    // back), 20.2 against 23.0 to FP8, 33.2 against 36.4 from fp32.  A read has too little of that to gain: 15.1 us
+    // either way for twice the tokens, FP8 17.9 against 17.3.
     while (chunks == 2 && (1u << g.row_shift) < g.per_row) ++g.row_shift;
     g.waves = writes && chunks == 2 && (1u << g.row_shift) == g.per_row && g.per_row <= 64 && c.heads % (64 / g.per_row) == 0;
     if (g.waves) {
@@ -605,7 +607,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t st)
     const uint32_t n = a.bf16 ? 8 : 4, hr = a.r.rot / 2;
     const bool strides = a.ldx_t % n == 0 && a.ldx_h % n == 0 && a.ldy_t % n == 0 && a.ldy_h % n == 0;
     // Pairs on whole chunks: interleaved ones lie inside a chunk, halves are whole chunks apart.  8192 x 64 heads
-    // of 128, bf16: 47 us against 108 pair by pair, half of each interleaved 46 against 178.
+    // of 128, bf16: 47 us against 104 pair by pair, half of each interleaved 45 against 176.
     const bool whole = strides && a.dim % n == 0 && (a.r.inter ? a.r.rot % n == 0 : hr % n == 0);
     kv::RopeGrid g{};
     g.rot_units = hr / n;
@@ -676,8 +678,8 @@ hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t st)
 {
     const uint32_t rope = a.r.table && a.r.rot ? ((a.r.inter ? a.r.rot % 8 == 0 : a.r.rot % 16 == 0) ? 1u : 2u) : 0u;
     // Two chunks a thread where every half row is whole blocks; a rotated key's halves are those of its
-    // rotated part and of the rest.  With one a pair's other half comes from another thread: 22.6 us against 17.9
-    // for 8192 x 8 heads of 128, FP8 26.4 against 22.0.
+    // rotated part and of the rest.  With one a pair's other half comes from another thread: 22.1 us against 17.1
+    // for 8192 x 8 heads of 128, FP8 25.0 against 20.2.
     const uint32_t rot = rope == 1 && !a.r.inter ? a.r.rot : 0u;
     const bool two = a.c.dim / 2 % a.c.block == 0 && rot / 2 % a.c.block == 0 && (a.c.dim - rot) / 2 % a.c.block == 0;
     kv::KvGrid g = kv::kv_grid(a.c, a.tokens, two ? 2 : 1, 2, true);

@@ -24,17 +24,18 @@
 // are fp32.  The product with the values takes bf16, in which codes times scales are exact and p is not: p goes
 // in as two parts, its nearest bf16 and the nearest bf16 of the rest, which leaves 2^-16 of it.  One part, 2^-8
 // of a term, was as large an error as the rounding of the result, which is the only one to bf16 now.  The second
-// products are free where memory is waited for (32 sequences up to 8192: 41.9 and 42.3 us) and cost the
-// many-row cases 13 to 18% (8 trees over FP8: 68.7 and 77.7 us; 512 rows of a head over 131072 tokens: 389 and 458).
+// products are free where memory is waited for (32 sequences up to 8192: 41.9 and 42.4 us) and cost the
+// many-row cases 13 to 22% (8 trees over FP8: 68.2 and 77.7 us; 512 rows of a head over 131072 tokens: 390 and 462).
 //
-// What bounds it.  Few rows (decode): HBM, 5.3 TB/s of FP4 and 5.8 of FP8 per added token, and some 6 us of
-// loads that wait for each other before the first tile and after the last.  Many rows: issue.  Over FP4 a tile
-// of 32 tokens x 32 rows x 128 elements takes 32 MFMAs (512 cycles) and 230 other vector instructions (64 to
-// decode, 32 to pair tokens, 16 exponentials), for two waves of a SIMD: vector units 49%, matrix
-// units 28% of the cycles, 0.6 PFLOP/s at a clock that falls to 2.2 GHz.  What was tried there and measured
-// alike: decoding a pair of elements between the products of the last, table entries read a tile
+// What bounds it.  Few rows (decode): HBM, 5.4 TB/s of FP4 and 5.9 of FP8 per added token (32 sequences of 8192
+// and of 16384: 71.8 and 124.5 us, 115.3 and 209.5), besides some 20 us of a call: two launches, loads that wait
+// for each other before the first tile and after the last, workgroups that end at different times.  Many rows:
+// issue.  Over FP4 a tile of 32 tokens x 32 rows x 128 elements takes 48 MFMAs (768 cycles) and 277 other vector
+// instructions (64 to decode, 32 to pair tokens, 16 exponentials, 48 to split p), for two waves of a SIMD: vector
+// units 54%, matrix units 37% of the cycles, 0.60 PFLOP/s at a clock that falls to 2.1 GHz.  What was tried there
+// and measured alike: decoding a pair of elements between the products of the last, table entries read a tile
 // ahead, all LDS reads before the first use, two or four waves on one tile behind a barrier, Q in LDS with three
-// waves of a SIMD.  64 rows of a wave spill: twice the time.
+// waves of a SIMD.  64 rows of a wave spill: 2.6 times the time.
 #pragma once
 
 #include <type_traits>
@@ -131,7 +132,7 @@ struct Cut {
 // Teams that a list of `units` is shared by: all, unless that leaves them fewer than 3 units and every CU has a
 // workgroup without them.  A piece costs its beginning, its end and its part of the join: one head's 8 rows over
 // 131072 FP4 tokens took 13 + 12 us by 342 workgroups and 15 + 22 by 768; 8 heads over 2047 are best off with a
-// unit each (6.7 + 5.0 us, with 3 units 8.2 + 4.5).
+// unit each (6.6 + 5.3 us, with 3 units 8.4 + 4.8).
 __device__ __forceinline__ uint32_t teams_for(const AttnPlan& p, uint32_t units)
 {
     const uint32_t few = 256 / p.team, n = units / 3 > few ? units / 3 : few;
@@ -279,8 +280,8 @@ __device__ __forceinline__ void wait_loads()  // all but the N newest vector loa
 //  * Scales: (key half 0, key half 1, value half 0, value half 1) x 16 rows x bytes of a row.
 // SPREAD: 0 where pages are whole numbers of 16 tokens, so that a half's rows are neighbours; 1 where rows are
 // found one by one; 2 where moreover a row has one or two scale bytes, which are loaded one by one, four LDS
-// bytes each.  200 rows x 8000 tokens of 128 FP8 elements under 16-element scales: 79 us with pages of 64, with
-// pages of 100 92 us by words and 160 byte by byte.
+// bytes each.  200 rows x 8000 tokens of 128 FP8 elements under 16-element scales: 88 us with pages of 64, with
+// pages of 100 98 us by words (byte by byte they took 1.7 times as long).
 template <bool FP8, int D, int BS, int SPREAD>
 struct Stage {
     static constexpr int RB = FP8 ? D : D / 2;        // bytes of a row
@@ -607,8 +608,8 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
     const Cut cut{total / teams, total % teams};
     // Workgroups go to the 8 XCDs in turn: numbered so that those of an XCD, and with them those of a team, are
     // neighbours and find in its L2 what one of them has read: 8 x 16384 FP8 tokens with 192 rows for each of 8
-    // heads took 187 us in place of 247, when next to no read of a second row tile was a hit.  Teams of one have
-    // nothing to share and keep the turn (64 x up to 4096 FP4 tokens: 37.4 us, as neighbours 38.9).
+    // heads take 210 us in place of 270, when next to no read of a second row tile is a hit.  Teams of one have
+    // nothing to share and keep the turn (64 x up to 4096 FP4 tokens: 45.0 us, as neighbours 46.9).
     const uint32_t xcd = blockIdx.x & 7, each = gridDim.x >> 3, more = gridDim.x & 7;
     const uint32_t group = p.team == 1 ? blockIdx.x : xcd * each + (xcd < more ? xcd : more) + (blockIdx.x >> 3);
     const uint32_t team = group / p.team, member = group - team * p.team;
@@ -788,7 +789,7 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
                 wait_loads<0>();
             }
             // Of two workgroups of a CU the older is served first, and ends early: they take turns in front,
-            // four tiles each (512 rows of a head over 131072 FP4 tokens: 488 to 458 us).  Fewer rows, which wait
+            // four tiles each (512 rows of a head over 131072 FP4 tokens: 485 to 462 us, FP8 495 to 490).  Fewer rows, which wait
             // for memory, gained nothing.
             if constexpr (NQ * D == 256) {
                 if (((k >> 2) + (blockIdx.x >> 8)) & 1) __builtin_amdgcn_s_setprio(0);
@@ -1015,7 +1016,7 @@ __global__ __launch_bounds__(256, (Room<FP8, D, BS, NQ, SPREAD>::GROUPS)) void a
 
 // Joins the pieces of the segments that were cut: a workgroup takes elements j0 ... j0 + JW - 1 of
 // every run of D / 16 of 16 rows, its waves every WAVES-th piece, four at a time; all are added in
-// an order that the lengths fix.  5 to 8 us, most of it the launch and three loads that wait for each other.
+// an order that the lengths fix.  4 to 8 us, most of it the launch and three loads that wait for each other.
 template <int D, int NQ, int WAVES, int JW>
 __global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(KvAttnArgs a, AttnPlan p)
 {

@@ -116,7 +116,7 @@ constexpr uint32_t MOST_GROUPS = 256 * 4, MOST_TEAM = 16;
 bool on_matrix_cores(const KvPool& c) { return c.dim == 64 || c.dim == 128 || c.dim == 256; }
 
 // 16-row tiles that a workgroup works on together: as many as the rows fill, since they share a token's decoded
-// key and value, up to what the registers hold: 4096 sums of a wave's rows (8192 spill: 1023 us against 478 for
+// key and value, up to what the registers hold: 4096 sums of a wave's rows (8192 spill: 1209 us against 462 for
 // 512 rows of a head of 128 over 131072 tokens)
 int row_tile(const KvAttnArgs& a)
 {
@@ -135,8 +135,8 @@ kv::AttnPlan plan_of(const KvAttnArgs& a)
     // a head's tiles, or an equal part of them
     const uint32_t parts = (p.row_tiles + MOST_TEAM - 1) / MOST_TEAM;
     p.team = parts ? (p.row_tiles + parts - 1) / parts : 1;
-    // What beginning and ending a segment costs, in steps.  64 sequences of up to 4096 FP4 tokens, one row tile: 39.6,
-    // 37.4 and 38.2 us with 1, 2 and 3; 8 trees over up to 16384 FP8 tokens: 81, 69, 68 and 68 with 2, 3, 4 and 6.
+    // What beginning and ending a segment costs, in steps.  64 sequences of up to 4096 FP4 tokens, one row tile: 47.1,
+    // 45.0 and 46.0 us with 1, 2 and 3; 8 trees over up to 16384 FP8 tokens: 87, 81, 79 and 83 with 2, 3, 4 and 6.
     p.begin = nq == 1 ? 2 : 4;
     const uint64_t longest = ((uint64_t)a.max_pages * a.c.page + kv::STEP - 1) / kv::STEP;
     p.most = (uint64_t)a.batch * ((a.c.heads * p.row_tiles + p.team - 1) / p.team) * ((longest ? longest : 1) + p.begin);
