@@ -9,11 +9,14 @@ def made_on(stream, make, *args, **kw) -> torch.Tensor:
     kernels run.  Memory of the current stream could still be in use there, or be given to others there as
     soon as the call returns, while the kernels are still to run.  The current stream is recorded as a user:
     a result that is dropped is not given to others before that stream's work on it is done."""
-    if stream is None:
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
         return make(*args, **kw)
     current = torch.cuda.current_stream()
-    with torch.cuda.stream(stream):
+    torch.cuda.set_stream(stream)  # as torch.cuda.stream does, in less of the host's time
+    try:
         t = make(*args, **kw)
+    finally:
+        torch.cuda.set_stream(current)
     if t.is_cuda:
         t.record_stream(current)
     return t

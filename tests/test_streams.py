@@ -1,7 +1,6 @@
 """Calls that are given a stream: the tensors that they make themselves are memory of that stream, also where
 the current stream is busy with the memory that it would hand out.  On the CPU by stand-ins for the library
 and the allocator's stream, on the GPU by two streams at once."""
-import contextlib
 from types import SimpleNamespace
 
 import numpy as np
@@ -30,24 +29,22 @@ class Library:
 @pytest.fixture
 def made(monkeypatch):
     """The streams that tensors were made on, in order; CPU tensors pass for a GPU's."""
-    on, inside = [], [None]
+    on, current = [], [SimpleNamespace(cuda_stream=11, device_index=0)]
+    usual = current[0]
 
-    @contextlib.contextmanager
-    def stream(s):
-        inside.append(s)
-        yield
-        inside.pop()
+    def set_stream(s):
+        current[0] = s
 
     def noted(make):
         def call(*args, **kw):
-            on.append(inside[-1])
+            on.append(None if current[0] is usual else current[0])
             kw.pop("device", None)
             return make(*args, **kw)
         return call
 
     library = Library()
-    monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=11, device_index=0))
+    monkeypatch.setattr(torch.cuda, "set_stream", set_stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[0])
     for name in ("empty", "empty_like", "zeros"):
         monkeypatch.setattr(torch, name, noted(getattr(torch, name)))
     new_empty = torch.Tensor.new_empty
@@ -56,10 +53,11 @@ def made(monkeypatch):
     monkeypatch.setattr(kv, "_on_gpu", lambda t: 0)
     monkeypatch.setattr(kv, "_same_device", lambda *a: None)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 11, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: current[0].cuda_stream, raising=False)
     monkeypatch.setattr(mx, "lib", lambda: library)
     monkeypatch.setattr(mx, "_need_gpu", lambda **kw: None)
-    return SimpleNamespace(on=on, calls=library.calls)
+    yield SimpleNamespace(on=on, calls=library.calls)
+    assert current[0] is usual
 
 
 def kv_calls():
@@ -114,6 +112,13 @@ def test_weight_calls_make_their_tensors_on_the_given_stream(made, name, monkeyp
     made.on.clear()
     call()
     assert made.on == [None] * count and made.calls[-1][1][-1] == 11
+
+
+def test_the_current_stream_given_is_as_none_given(made):
+    for count, call in kv_calls().values():
+        made.on.clear()
+        call(stream=SimpleNamespace(cuda_stream=11, device_index=0))
+        assert made.on == [None] * count and made.calls[-1][1][-1] == 11
 
 
 def test_cache_calls_refuse_a_stream_of_another_gpu(made):
