@@ -11,12 +11,13 @@ def made_on(stream, make, *args, **kw) -> torch.Tensor:
     a result that is dropped is not given to others before that stream's work on it is done."""
     if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
         return make(*args, **kw)
-    current = torch.cuda.current_stream()
-    torch.cuda.set_stream(stream)  # as torch.cuda.stream does, in less of the host's time
-    try:
-        t = make(*args, **kw)
-    finally:
-        torch.cuda.set_stream(current)
+    current = torch.cuda.current_stream(stream.device_index)
+    with torch.cuda.device(stream.device_index):
+        torch.cuda.set_stream(stream)  # as torch.cuda.stream does, in less of the host's time
+        try:
+            t = make(*args, **kw)
+        finally:
+            torch.cuda.set_stream(current)
     if t.is_cuda:
         t.record_stream(current)
     return t

@@ -1,6 +1,7 @@
 """Calls that are given a stream: the tensors that they make themselves are memory of that stream, also where
 the current stream is busy with the memory that it would hand out.  On the CPU by stand-ins for the library
 and the allocator's stream, on the GPU by two streams at once."""
+import contextlib
 from types import SimpleNamespace
 
 import numpy as np
@@ -43,6 +44,7 @@ def made(monkeypatch):
         return call
 
     library = Library()
+    monkeypatch.setattr(torch.cuda, "device", contextlib.nullcontext)
     monkeypatch.setattr(torch.cuda, "set_stream", set_stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[0])
     for name in ("empty", "empty_like", "zeros"):
